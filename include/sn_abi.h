@@ -171,12 +171,16 @@ sn_status sn_ctx_create(int32_t device, SnCtx** out_ctx);
  * streams that still use it. */
 void sn_ctx_free(SnCtx* ctx);
 
-/* Hand the context a caller-owned device workspace (used only by the chunked
- * look-back scan).  `dev_ptr` must be 256-byte aligned; `bytes` >= 0; a NULL
+/* Hand the context a caller-owned device workspace (used by the chunked scans
+ * and recurrences, and by the operators around the recurrent layer that say
+ * so).  `dev_ptr` must be 256-byte aligned; `bytes` >= 0; a NULL
  * pointer or 0 bytes removes it.  The library never frees it.  The first
- * look-back launch after this call (or after another chunked path used the
- * workspace) clears the flag and carry-word areas with cudaMemsetAsync on that
- * launch's stream. */
+ * look-back or fused scan after this call (or after another kind of call used
+ * the workspace) clears its flag and carry words with cudaMemsetAsync on that
+ * launch's stream.  A captured one always does, as part of its graph; and once
+ * a captured call writes this context's workspace, so does every look-back or
+ * fused scan of another layout outside of a graph, because a replay may have
+ * come before it. */
 sn_status sn_ctx_set_workspace(SnCtx* ctx, void* dev_ptr, int64_t bytes);
 
 /* Workspace bytes the chunked scans need for this problem (op =
@@ -217,7 +221,8 @@ sn_status sn_ctx_get_option(SnCtx* ctx, int32_t key, int32_t* value);
  * bits, are deterministic and are bit-exact under splits at multiples of
  * SN_OPT_LOOKBACK_CHUNK.  Calls may be captured in a CUDA graph and replayed:
  * the look-back and fused kernels keep their launch epoch in device memory,
- * so every replay tags its flags and carry words afresh.
+ * so every replay tags its flags and carry words afresh, and the graph clears
+ * them first, so that any call on the context may come between replays.
  * Pointers need 4-byte alignment; N % 4 == 0 with 16-byte aligned a, b and
  * s_out enables the TMA path.  Errors: SN_E_INVAL, SN_E_NOMEM (look-back
  * forced without enough workspace), SN_E_DEVICE. */

@@ -86,6 +86,47 @@ struct DeviceGuard {
     }
 };
 
+// Whether `s` is being captured into a CUDA graph.
+bool capturing(cudaStream_t s) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+        cudaGetLastError();   // the legacy stream beside a capture: the launch behind answers for it
+        return false;
+    }
+    return st == cudaStreamCaptureStatusActive;
+}
+
+// The tagged words of the look-back and fused scans trust what lies in the
+// workspace: stale words of earlier launches never carry a later epoch, other
+// data might (a token number of the embedding gradient's sort is a small
+// integer like a tag).  ws_dirty and lb_last_flags say what lies there only
+// while calls run once, in the order they are made.  A captured call runs
+// whenever its graph is replayed, so
+//   - a captured scan clears its words within the graph;
+//   - outside of one, a scan clears them at every call once a graph holds a
+//     writer of the workspace other than scans of its own layout (graph_sig).
+constexpr int64_t kGraphMixed = INT64_MIN;
+
+// A call that leaves data of its own in the workspace.
+void ws_overwritten(SnCtx* c, cudaStream_t s) {
+    c->ws_dirty = true;
+    if (capturing(s)) c->graph_sig = kGraphMixed;
+}
+
+// Whether a scan whose tagged words are laid out as `sig` has to clear them.
+bool ws_needs_clear(const SnCtx* c, int64_t sig, bool captured) {
+    return captured || c->ws_dirty || c->lb_last_flags != sig || (c->graph_sig != 0 && c->graph_sig != sig);
+}
+// Such a scan has been enqueued, with the clearing that it needed.
+void ws_tagged(SnCtx* c, int64_t sig, bool captured) {
+    if (captured) {
+        c->graph_sig = c->graph_sig == 0 || c->graph_sig == sig ? sig : kGraphMixed;
+    } else {
+        c->ws_dirty = false;
+        c->lb_last_flags = sig;
+    }
+}
+
 uint64_t wait_ns(const SnCtx* c) { return (uint64_t)c->wait_limit_us * 1000ull; }
 
 // The side streams and events of the pipelined chunked delta rule, created
@@ -270,6 +311,7 @@ sn_status sn_ctx_set_workspace(SnCtx* ctx, void* dev_ptr, int64_t bytes) {
     ctx->ws = dev_ptr;
     ctx->ws_bytes = bytes;
     ctx->ws_dirty = true;
+    if (ctx->graph_sig != 0) ctx->graph_sig = kGraphMixed;   // earlier graphs keep writing where it was
     return SN_OK;
 }
 
@@ -396,7 +438,8 @@ static sn_status scan_common(SnCtx* ctx, int32_t B, int32_t T, int32_t N, const 
     }
     if (kernel == SN_SCAN_KERNEL_LOOKBACK) {
         const int64_t nflags = lookback_flag_count(B, T, N);
-        if (ctx->ws_dirty || nflags != ctx->lb_last_flags) {
+        const bool captured = capturing(s);
+        if (ws_needs_clear(ctx, nflags, captured)) {
             // fresh flag and carry-word areas: zero them once, on the caller's
             // stream.  Between clears every launch rewrites all its flags and
             // carry words, and the launch epoch (kept on the device) differs
@@ -406,9 +449,8 @@ static sn_status scan_common(SnCtx* ctx, int32_t B, int32_t T, int32_t N, const 
                 cudaMemsetAsync(static_cast<char*>(ctx->ws) + cw_off, 0, (size_t)(need - cw_off), s) != cudaSuccess ||
                 cudaMemsetAsync(&ctx->dstatus->abort_tag, 0, sizeof(unsigned int), s) != cudaSuccess)
                 return SN_E_DEVICE;
-            ctx->ws_dirty = false;
-            ctx->lb_last_flags = nflags;
         }
+        ws_tagged(ctx, nflags, captured);
         return from_cuda(launch_scan_lookback(x, gated, ctx->ws, ctx->debug_poison, ctx->dstatus, wait_ns(ctx),
                                               ctx->sm_count, s));
     }
@@ -417,23 +459,23 @@ static sn_status scan_common(SnCtx* ctx, int32_t B, int32_t T, int32_t N, const 
         // carry words tagged with the look-back kernel's launch epoch, in other
         // places: cleared when the workspace, the geometry or the user changes
         const int64_t sig = -lookback_flag_count(B, T, N);
-        if (ctx->ws_dirty || ctx->lb_last_flags != sig) {
+        const bool captured = capturing(s);
+        if (ws_needs_clear(ctx, sig, captured)) {
             int64_t ta, tb;
             scan_fused_tag_area(B, T, N, &ta, &tb);
             if (cudaMemsetAsync(static_cast<char*>(ctx->ws) + ta, 0, (size_t)tb, s) != cudaSuccess ||
                 cudaMemsetAsync(&ctx->dstatus->abort_tag, 0, sizeof(unsigned int), s) != cudaSuccess)
                 return SN_E_DEVICE;
-            ctx->ws_dirty = false;
-            ctx->lb_last_flags = sig;
         }
+        ws_tagged(ctx, sig, captured);
         bool fell_back = false;
         const cudaError_t e = launch_scan_fused(x, gated, ctx->ws, ctx->debug_poison, ctx->dstatus, wait_ns(ctx),
                                                 ctx->sm_count, s, &fell_back);
-        if (fell_back) ctx->ws_dirty = true;   // reduce-then-scan's arrays overwrote the tagged words
+        if (fell_back) ws_overwritten(ctx, s);   // reduce-then-scan's arrays overwrote the tagged words
         return from_cuda(e);
     }
     if (kernel == SN_SCAN_KERNEL_REDUCE_SCAN) {
-        ctx->ws_dirty = true;   // its carries overwrite the look-back's carry words
+        ws_overwritten(ctx, s);   // its carries overwrite the look-back's carry words
         return from_cuda(launch_scan_reduce_scan(x, gated, ctx->ws, ctx->dstatus, wait_ns(ctx), ctx->sm_count, s));
     }
     return from_cuda(launch_scan_sequential(x, gated, ctx->dstatus, wait_ns(ctx), s));
@@ -584,7 +626,7 @@ static sn_status scan_backward_common(SnCtx* ctx, BwdArgs& x, bool gated, void* 
     if (!g.ok) return SN_E_DEVICE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (chunked) {
-        ctx->ws_dirty = true;   // the carries overwrite the look-back flag area
+        ws_overwritten(ctx, s);   // the carries overwrite the look-back flag area
         return from_cuda(launch_scan_backward_chunked(x, gated, ctx->ws, ctx->dstatus, wait_ns(ctx), ctx->sm_count, s));
     }
     return from_cuda(launch_scan_backward(x, gated, ctx->dstatus, wait_ns(ctx), s));
@@ -702,7 +744,7 @@ sn_status sn_recur_diag_chunked(SnCtx* ctx, int32_t B, int32_t T, int32_t H, int
     if (ctx->ws == nullptr || ctx->ws_bytes < need) return SN_E_NOMEM;
     DeviceGuard g(ctx->device);
     if (!g.ok) return SN_E_DEVICE;
-    ctx->ws_dirty = true;   // the chunk states overwrite the look-back flag area
+    ws_overwritten(ctx, reinterpret_cast<cudaStream_t>(stream));   // the chunk states overwrite the look-back flag area
     return from_cuda(launch_recur_chunked(x, ctx->ws, ctx->dstatus, wait_ns(ctx), ctx->sm_count,
                                           reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -722,7 +764,7 @@ sn_status sn_recur_delta_chunked(SnCtx* ctx, int32_t B, int32_t T, int32_t H, in
     if (ctx->ws == nullptr || ctx->ws_bytes < need) return SN_E_NOMEM;
     DeviceGuard g(ctx->device);
     if (!g.ok) return SN_E_DEVICE;
-    ctx->ws_dirty = true;   // the chunk tiles overwrite the look-back flag area
+    ws_overwritten(ctx, reinterpret_cast<cudaStream_t>(stream));   // the chunk tiles overwrite the look-back flag area
     const DeltaPipe pipe{ctx->pipe_prep, ctx->pipe_chain, ctx->pipe_out, ctx->pipe_ev, 20};
     return from_cuda(launch_delta_chunked(x, ctx->ws, ctx->dstatus, wait_ns(ctx), ctx->sm_count, ctx->delta_segments,
                                           ctx->debug_poison != 0, pipe, reinterpret_cast<cudaStream_t>(stream)));
@@ -850,7 +892,7 @@ sn_status sn_embed_backward(SnCtx* ctx, int32_t n, int32_t V, int32_t D, int32_t
     if (ctx->ws == nullptr || ctx->ws_bytes < need) return SN_E_NOMEM;
     DeviceGuard g(ctx->device);
     if (!g.ok) return SN_E_DEVICE;
-    ctx->ws_dirty = true;   // the sort overwrites the look-back flag area
+    ws_overwritten(ctx, reinterpret_cast<cudaStream_t>(stream));   // the sort overwrites the look-back flag area
     const EmbedBwdArgs x{n, V, D, dtype, grad_dtype, ids_type, ids, grad_out, scale, accumulate, grad_table};
     return from_cuda(launch_embed_backward(x, ctx->ws, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -899,7 +941,7 @@ sn_status sn_add_rmsnorm_backward(SnCtx* ctx, int32_t R, int32_t D, int32_t dtyp
     if (dw != nullptr && (ctx->ws == nullptr || ctx->ws_bytes < need)) return SN_E_NOMEM;
     DeviceGuard g(ctx->device);
     if (!g.ok) return SN_E_DEVICE;
-    if (dw != nullptr) ctx->ws_dirty = true;   // the partial sums overwrite the look-back flag area
+    if (dw != nullptr) ws_overwritten(ctx, reinterpret_cast<cudaStream_t>(stream));   // the partial sums overwrite the look-back flag area
     const RmsNormBwdArgs a{R, D, dtype, dy_dtype, dy, h, w, rstd, dh, dx, dw};
     return from_cuda(launch_add_rmsnorm_backward(a, ctx->ws, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -926,7 +968,7 @@ static sn_status linear_ce_common(SnCtx* ctx, const LinearCeArgs& x, void* strea
     if (ctx->ws == nullptr || ctx->ws_bytes < need) return SN_E_NOMEM;
     DeviceGuard g(ctx->device);
     if (!g.ok) return SN_E_DEVICE;
-    ctx->ws_dirty = true;   // the tiles' results overwrite the look-back flag area
+    ws_overwritten(ctx, reinterpret_cast<cudaStream_t>(stream));   // the tiles' results overwrite the look-back flag area
     return from_cuda(launch_linear_ce(x, ctx->ws, ctx->dstatus, wait_ns(ctx), reinterpret_cast<cudaStream_t>(stream)));
 }
 
