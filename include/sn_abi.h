@@ -116,6 +116,8 @@ typedef int32_t sn_status;
                                       chains (one CTA per head and batch row) leave at least half the SMs,
                                       else a segmented pipeline; or 1..8 segments of the chunk sequence run
                                       as a pipeline (same bits for every value) */
+#define SN_OPT_WORKSPACE_CAPTURED 8 /* read-only: 1 once a captured call uses the present workspace, whose
+                                      memory then has to stay as long as the graph */
 
 #define SN_SCAN_KERNEL_AUTO       0
 #define SN_SCAN_KERNEL_SEQUENTIAL 1
@@ -180,7 +182,8 @@ void sn_ctx_free(SnCtx* ctx);
  * launch's stream.  A captured one always does, as part of its graph; and once
  * a captured call writes this context's workspace, so does every look-back or
  * fused scan of another layout outside of a graph, because a replay may have
- * come before it. */
+ * come before it.  A graph keeps the address of the workspace that its calls
+ * were captured with: that memory has to outlive the graph. */
 sn_status sn_ctx_set_workspace(SnCtx* ctx, void* dev_ptr, int64_t bytes);
 
 /* Workspace bytes the chunked scans need for this problem (op =
@@ -200,7 +203,8 @@ int64_t sn_workspace_bytes(int32_t op, int32_t B, int32_t T, int32_t N);
 sn_status sn_ctx_last_error(SnCtx* ctx);
 
 /* Set / read a context option (SN_OPT_*).  SN_E_INVAL for an unknown key or
- * out-of-range value; SN_OPT_LOOKBACK_CHUNK is read-only. */
+ * out-of-range value; SN_OPT_LOOKBACK_CHUNK and SN_OPT_WORKSPACE_CAPTURED are
+ * read-only. */
 sn_status sn_ctx_set_option(SnCtx* ctx, int32_t key, int32_t value);
 sn_status sn_ctx_get_option(SnCtx* ctx, int32_t key, int32_t* value);
 

@@ -45,6 +45,7 @@ class Context:
         _check(s, "sn_ctx_create")
         self.handle = h
         self._ws = None
+        self._kept = []
         self._lib = _abi.load()
         self._dev, self._empty, self._f32 = torch.device("cuda", device), torch.empty, torch.float32
         self._raw_stream = torch._C._cuda_getCurrentRawStream
@@ -77,16 +78,17 @@ class Context:
 
     def ensure_workspace(self, B: int, T: int, N: int) -> None:
         """Give the context enough workspace for the look-back scan of (B, T, N)."""
-        need = _abi.sn_workspace_bytes(_abi.SN_OP_SCAN_FMA, B, T, N)
-        if self._ws is not None and self._ws.numel() >= need:
-            return
-        self._ws = self._torch.empty(max(need, 256), dtype=self._torch.uint8, device=f"cuda:{self.device}")
-        _check(_abi.sn_ctx_set_workspace(self.handle, self._ws, self._ws.numel()), "sn_ctx_set_workspace")
+        self.ensure_workspace_bytes(_abi.sn_workspace_bytes(_abi.SN_OP_SCAN_FMA, B, T, N))
 
     def ensure_workspace_bytes(self, need: int) -> None:
-        """Give the context a workspace of at least `need` bytes."""
+        """Give the context a workspace of at least `need` bytes.  One that a
+        captured call uses is kept beside the new one as long as the context
+        lives, because the graph writes to it at every replay; ask for the
+        most that will be needed before a capture to have a single one."""
         if self._ws is not None and self._ws.numel() >= need:
             return
+        if self._ws is not None and self.get_option(_abi.SN_OPT_WORKSPACE_CAPTURED):
+            self._kept.append(self._ws)
         self._ws = self._torch.empty(max(need, 256), dtype=self._torch.uint8, device=f"cuda:{self.device}")
         _check(_abi.sn_ctx_set_workspace(self.handle, self._ws, self._ws.numel()), "sn_ctx_set_workspace")
 

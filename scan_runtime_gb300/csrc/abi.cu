@@ -110,7 +110,9 @@ constexpr int64_t kGraphMixed = INT64_MIN;
 // A call that leaves data of its own in the workspace.
 void ws_overwritten(SnCtx* c, cudaStream_t s) {
     c->ws_dirty = true;
-    if (capturing(s)) c->graph_sig = kGraphMixed;
+    if (!capturing(s)) return;
+    c->graph_sig = kGraphMixed;
+    c->ws_in_graph = true;
 }
 
 // Whether a scan whose tagged words are laid out as `sig` has to clear them.
@@ -121,6 +123,7 @@ bool ws_needs_clear(const SnCtx* c, int64_t sig, bool captured) {
 void ws_tagged(SnCtx* c, int64_t sig, bool captured) {
     if (captured) {
         c->graph_sig = c->graph_sig == 0 || c->graph_sig == sig ? sig : kGraphMixed;
+        c->ws_in_graph = true;
     } else {
         c->ws_dirty = false;
         c->lb_last_flags = sig;
@@ -311,6 +314,7 @@ sn_status sn_ctx_set_workspace(SnCtx* ctx, void* dev_ptr, int64_t bytes) {
     ctx->ws = dev_ptr;
     ctx->ws_bytes = bytes;
     ctx->ws_dirty = true;
+    ctx->ws_in_graph = false;
     if (ctx->graph_sig != 0) ctx->graph_sig = kGraphMixed;   // earlier graphs keep writing where it was
     return SN_OK;
 }
@@ -374,6 +378,7 @@ sn_status sn_ctx_get_option(SnCtx* ctx, int32_t key, int32_t* value) {
         case SN_OPT_RECUR_KERNEL: *value = ctx->recur_kernel; return SN_OK;
         case SN_OPT_RECUR_TILE: *value = ctx->recur_tile; return SN_OK;
         case SN_OPT_DELTA_SEGMENTS: *value = ctx->delta_segments; return SN_OK;
+        case SN_OPT_WORKSPACE_CAPTURED: *value = ctx->ws_in_graph ? 1 : 0; return SN_OK;
         default: return SN_E_INVAL;
     }
 }

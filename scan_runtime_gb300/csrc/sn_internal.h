@@ -40,6 +40,7 @@ struct SnCtx {
     bool ws_dirty;              // flag area must be cleared before next use
     int64_t lb_last_flags;      // layout of the tagged flags last cleared: the look-back kernel's flag
                                 // count, or minus the fused path's tile count
+    bool ws_in_graph;           // a captured call uses this workspace
     int64_t graph_sig;          // captured calls that write the workspace: 0 none, the lb_last_flags of the
                                 // only such scans, or INT64_MIN for any other mix
     uint64_t tagged_calls;      // look-back and fused launches since the tagged words were last cleared

@@ -149,3 +149,66 @@ def test_a_capture_alone_clears_nothing(sr, ctx):
     assert torch.equal(ctx.scan_fma(a, b)[0], want)
     graph.replay()
     assert torch.equal(out, want)
+
+
+def _beyond(x, y):
+    return x.data_ptr() + x.numel() <= y[0] or y[0] + y[1] <= x.data_ptr()
+
+
+def test_a_grown_workspace_leaves_graphs_theirs(sr, ctx):
+    """A step captured with a small workspace, then a call that needs a larger
+    one: the memory that the graph writes belongs to nobody else, and it still
+    gives the step's bits."""
+    g = torch.Generator("cuda").manual_seed(8)
+    h, w = (torch.randn(s, 128, generator=g, device="cuda").to(BF16) for s in (3, 700))
+    t = torch.tensor([0, 5, 699], device="cuda")
+    assert ctx.get_option(sr.SN_OPT_WORKSPACE_CAPTURED) == 0
+    want, _ = ctx.linear_ce(h, w, t)
+    torch.cuda.synchronize()
+    assert ctx.get_option(sr.SN_OPT_WORKSPACE_CAPTURED) == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, _ = ctx.linear_ce(h, w, t)
+    assert ctx.get_option(sr.SN_OPT_WORKSPACE_CAPTURED) == 1
+    old = ctx._ws.data_ptr(), ctx._ws.numel()
+    embed, _ = _operators(ctx)
+    dtable = embed()
+    assert ctx._ws.numel() > old[1] and ctx.get_option(sr.SN_OPT_WORKSPACE_CAPTURED) == 0
+    others = [torch.full((old[1],), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    assert all(_beyond(x, old) for x in others)
+    graph.replay()
+    assert torch.equal(loss, want) and all(bool((x == 7).all()) for x in others)
+    assert torch.equal(embed(), dtable)
+    with pytest.raises(sr.SnError):
+        ctx.set_option(sr.SN_OPT_WORKSPACE_CAPTURED, 0)
+
+
+def test_a_workspace_of_no_graph_is_not_kept(sr, ctx):
+    for n in (1 << 12, 1 << 14, 1 << 16):
+        ctx.ensure_workspace_bytes(n)
+    assert ctx._kept == []
+
+
+@pytest.mark.parametrize("which", [0, 1], ids=["look-back", "fused"])
+def test_scan_replayed_across_a_growth(sr, ctx, which):
+    """The scan's graph stays with the workspace that it was captured with, the
+    calls behind it with the new one."""
+    _room(sr, ctx)
+    ctx.set_option(sr.SN_OPT_SCAN_KERNEL, _kernels(sr)[which][1])
+    embed, head = _operators(ctx)
+    a, b = _scan_inputs(9)
+    want, _ = ctx.scan_fma(a, b)
+    dtable = embed()
+    ctx.scan_fma(a, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = ctx.scan_fma(a, b)
+    ctx.ensure_workspace_bytes(1 << 27)
+    assert len(ctx._kept) == 1
+    for _ in range(3):
+        assert torch.equal(embed(), dtable)
+        graph.replay()
+        assert torch.equal(out, want)
+        assert torch.equal(ctx.scan_fma(a, b)[0], want)
+        head()
