@@ -273,13 +273,17 @@ class Context:
         return given, self._in(what, given, shape, dtype)
 
     def _on(self, stream, *tensors):
-        """The stream's handle (default: the current one of this device).  On
-        another stream than the current one, tells the allocator of the
-        tensors' use there, so that it does not hand their memory out early."""
+        """The handle of a stream given as such or as a torch stream (default:
+        the current one of this device).  On another stream than the current
+        one, tells the allocator of the tensors' use there, so that it does not
+        hand their memory out early."""
         if stream is None:
             return self._raw_stream(self.device)
         if isinstance(stream, int):
-            return stream
+            if stream == self._raw_stream(self.device):
+                return stream
+            # (1 is another name of the default stream, whose handle is 0)
+            stream = self._torch.cuda.ExternalStream(0 if stream == 1 else stream, self._dev)
         if stream.cuda_stream != self._raw_stream(self.device):
             for t in tensors:
                 if t is not None:

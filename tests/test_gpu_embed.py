@@ -263,3 +263,26 @@ def test_refusals(ctx, sr):
         ctx.embed_backward(ids, go, 8, accumulate=True)
     with pytest.raises(sr.SnError):
         ctx.embed(ids[:0], table)
+
+
+@pytest.mark.parametrize("as_handle", [False, True])
+def test_memory_used_on_another_stream_is_not_handed_out(ctx, as_handle):
+    """The call's tensors are dropped while it still waits behind a busy
+    stream: their memory is not given to the next tensors."""
+    g = _gen(61)
+    n, V, D = 3000, 50, 96
+    ids = torch.randint(0, V, (n,), generator=g, device="cuda")
+    rows = _normal(g, n, D)
+    want = ctx.embed_backward(ids, rows, V)
+    used = rows.clone()
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)       # about 10 ms
+    got = ctx.embed_backward(ids, used, V, stream=s.cuda_stream if as_handle else s)
+    at = used.data_ptr()
+    del used
+    others = [torch.full((n, D), 9.0, device="cuda") for _ in range(8)]
+    assert s.query() or all(x.data_ptr() != at for x in others)
+    s.synchronize()
+    assert torch.equal(got, want)

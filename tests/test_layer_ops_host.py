@@ -49,3 +49,37 @@ def test_linear_ce_workspace(abi):
     # the logits are not kept: 16384 x 131072 of them would be 4.3 GB in bf16
     assert f(16384, 131072, 2048, 1, 1) < 1 << 30
     assert f(16384, 131072, 2048, 1, 0) < 1 << 28
+
+
+class _Torch:
+    """Streams without a GPU."""
+    class cuda:
+        class ExternalStream:
+            def __init__(self, handle, device=None):
+                self.cuda_stream = handle
+
+
+class _Tensor:
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, s):
+        self.streams.append(s.cuda_stream)
+
+
+@pytest.mark.parametrize("current", [0, 0x500])
+def test_tensors_used_on_another_stream_are_recorded_there(current):
+    """However the stream is given: as a torch stream or as its handle."""
+    from scan_runtime_gb300 import Context
+    ctx = Context.__new__(Context)
+    ctx.handle, ctx.device, ctx._dev, ctx._torch = None, 0, None, _Torch
+    ctx._raw_stream = lambda device: current
+    x, y = _Tensor(), _Tensor()
+    assert ctx._on(None, x, None, y) == current and ctx._on(current, x) == current
+    assert ctx._on(_Torch.cuda.ExternalStream(current), x) == current
+    assert x.streams == y.streams == []
+    assert ctx._on(0x700, x, None, y) == 0x700
+    assert x.streams == y.streams == [0x700]
+    assert ctx._on(_Torch.cuda.ExternalStream(0x900), x) == 0x900
+    assert x.streams == [0x700, 0x900]
+    assert ctx._on(1, y) == 0 and y.streams == [0x700] + [0] * (current != 0)
