@@ -12,6 +12,8 @@
 #include <initializer_list>
 #include <map>
 #include <mutex>
+#include <set>
+#include <tuple>
 #include <utility>
 
 #include <cudaTypedefs.h>
@@ -196,7 +198,8 @@ bool lookback_supported(const ScanArgs& x);
 
 namespace {
 std::mutex g_attr_mutex;
-std::map<std::pair<const void*, int>, int> g_attr;     // (kernel, device) -> occupancy (0 = attr only)
+std::set<std::pair<const void*, int>> g_smem_set;                       // (kernel, device)
+std::map<std::tuple<const void*, int, int, size_t>, int> g_occupancy;   // (kernel, device, threads, smem)
 }  // namespace
 
 cudaError_t set_smem_attr_once(const void* kern, size_t bytes) {
@@ -205,9 +208,9 @@ cudaError_t set_smem_attr_once(const void* kern, size_t bytes) {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(g_attr_mutex);
     const auto key = std::make_pair(kern, dev);
-    if (g_attr.count(key)) return cudaSuccess;
+    if (g_smem_set.count(key)) return cudaSuccess;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) g_attr[key] = 0;
+    if (e == cudaSuccess) g_smem_set.insert(key);
     return e;
 }
 
@@ -218,7 +221,7 @@ cudaError_t occupancy_once(const void* kern, int threads, size_t smem, int* out)
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(g_attr_mutex);
-    int& occ = g_attr[std::make_pair(kern, dev)];
+    int& occ = g_occupancy[std::make_tuple(kern, dev, threads, smem)];
     if (occ == 0) {
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem);
         if (e != cudaSuccess) return e;

@@ -72,7 +72,8 @@ int64_t lookback_flag_count(int B, int T, int N);
 // Opt `kern` into `bytes` of dynamic shared memory on the current device (once
 // per kernel and device; function attributes are per device).
 cudaError_t set_smem_attr_once(const void* kern, size_t bytes);
-// Resident CTAs per SM of `kern` on the current device (cached per device).
+// Resident CTAs per SM of `kern` in CTAs of `threads` threads and `smem` bytes of
+// dynamic shared memory on the current device (cached for each of them).
 cudaError_t occupancy_once(const void* kern, int threads, size_t smem, int* out);
 
 

@@ -263,3 +263,21 @@ def test_refusals(ctx, sr):
         ctx.add_rmsnorm(x.cpu(), eps=1e-6)
     with pytest.raises(sr.SnError):
         ctx.add_rmsnorm(x[:0], eps=1e-6)
+
+
+def test_the_grid_follows_the_width_alone(ctx):
+    """Calls of several widths run the same kernel in CTAs of different sizes;
+    each width's grid fills the GPU whatever width came first.  CTAs of half
+    the threads: at least twice as many of them."""
+    from tests._graph_nodes import nodes
+    grids = {}
+    for D in (4096, 2048, 1024, 4096, 2048):
+        x = torch.zeros(20000, D, dtype=BF16, device="cuda")
+        call = lambda: ctx.add_rmsnorm(x, x, None, eps=1e-6)    # noqa: E731
+        call()
+        (k,), _ = nodes(call)
+        threads = k.block[0] * k.block[1]
+        assert grids.setdefault(D, (k.grid[0], threads)) == (k.grid[0], threads)
+    (g1, t1), (g2, t2) = grids[4096], grids[2048]
+    assert t1 == 2 * t2 and g2 >= 2 * g1
+    assert grids[1024] == grids[2048]       # two rows a CTA
