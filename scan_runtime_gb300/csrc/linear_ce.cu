@@ -747,12 +747,17 @@ __global__ void __launch_bounds__(256) ce_join(int64_t rows, int D, int64_t ld, 
 int64_t r256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // k blocks (of 64) summed in tensor memory at a time.  Its fp32 sums are cut,
-// not rounded to nearest: a sum of n steps of 16 comes out short by about
-// n 2^-26 of itself (measured 1e-5 at 500 steps), always to the same side.
-// fp32 results, and logits in narrow tiles, therefore add segments of 32 steps
-// in registers, to the nearest.  Wide tiles have no registers for that and
-// take logits of up to 128 steps (D <= 2048; lse is then off by 7e-7 of
-// itself, measured); bf16 results need no segments.
+// not rounded to nearest: each step of 16 loses up to about 2^-24 of the running
+// sum, always to the same side (a sum of one sign that grows steadily comes out
+// short by about n 2^-26 of itself after n steps: measured 1e-5 at 500; one that
+// is large from its first steps on, as dh's with a target among them, by up to
+// 2^-24 a step).  fp32 results, and logits in narrow tiles, therefore add
+// segments of 32 steps in registers, to the nearest.  Wide tiles have no
+// registers for that and take logits of up to 128 steps (D <= 2048; lse is then
+// off by 7e-7 of itself, measured).  bf16 gradients, and the five small products
+// of fp32 ones, are summed whole, but at most MOST_BLOCKS at a time, longer sums
+// in splits that are added in fp32: 1024 steps cut 2^-14 at most, a thirtieth of
+// bf16's half step.
 constexpr int SEG = 8, WHOLE = 32;
 
 // dz of one piece of the vocabulary takes at most this much workspace.
@@ -782,7 +787,9 @@ Cut cut_for(int64_t M, int64_t N, int64_t kblocks, bool f32, bool may_wide, bool
     for (int i = may_wide ? 0 : 1; i < 4; ++i) {
         const int64_t nt = (N + widths[i] - 1) / widths[i];
         if (i > 1 && mt * nt > 4 * GROUPS) break;    // many tiles: the wider ones are better
-        for (int64_t s = 1; s <= (may_split ? 16 : 1) && (s == 1 || kblocks / s >= least_blocks(f32)); ++s) {
+        const int64_t least = may_split ? least_splits(kblocks) : 1;
+        for (int64_t s = least; s <= (may_split ? std::max<int64_t>(least, 16) : 1) &&
+                                (s == least || kblocks / s >= least_blocks(f32)); ++s) {
             const int64_t tiles = mt * nt * s, tail = tiles % GROUPS;
             const double k = (double)kblocks / s;
             double us = (tiles + GROUPS - 1) / GROUPS * (k * unit[f32][i] + 1.5);

@@ -13,6 +13,8 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int BK = 64;                 // k of one block: 128 bytes of bf16
 constexpr int SMS = 152;               // SMs of the GPU this library is for: fixes how sums are cut up
+constexpr int MOST_BLOCKS = 256;       // k blocks of a gradient that tensor memory sums at a time (see SEG in linear_ce.cu)
+constexpr int64_t least_splits(int64_t kblocks) { return (kblocks + MOST_BLOCKS - 1) / MOST_BLOCKS; }
 
 enum Epi : int { EPI_LSE = 0, EPI_DZ = 1, EPI_OUT = 2 };
 

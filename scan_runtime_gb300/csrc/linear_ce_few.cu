@@ -298,8 +298,11 @@ cudaError_t run_few(const CUtensorMap& ta, const CUtensorMap& ta128, const CUten
 
 int few_box(int N) { return N <= 16 ? 16 : FEW_ROWS; }
 
-// As many as give every SM an item, of at least four blocks each.
-int few_splits(int D, int kblocks) { return std::max(1, std::min(SMS / ((D + 127) / 128), kblocks / 4)); }
+// As many as give every SM an item, of at least four blocks each, or as a long
+// sum needs.
+int few_splits(int D, int kblocks) {
+    return std::max((int)least_splits(kblocks), std::min(SMS / ((D + 127) / 128), kblocks / 4));
+}
 
 cudaError_t launch_few(Epi epi, const CUtensorMap& ta, const CUtensorMap& ta128, const CUtensorMap& tb, const CeFew& g,
                        SnDevStatus* st, uint64_t limit, cudaStream_t s) {

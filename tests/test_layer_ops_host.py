@@ -51,6 +51,18 @@ def test_linear_ce_workspace(abi):
     assert f(16384, 131072, 2048, 1, 0) < 1 << 28
 
 
+def test_long_sums_of_the_gradients_are_cut(abi):
+    """Tensor memory cuts its sums, by up to 2^-24 a step of 16 terms: no long
+    sum is left in one piece, which shows in its slices."""
+    f = abi.sn_linear_ce_workspace_bytes
+    # dw over 2^20 rows: 16 slices of (256, D) beside the packed h and dz
+    N, V, D = 1 << 20, 256, 38912
+    assert f(N, V, D, 1, 1) >= N * D * 2 + N * V * 2 + 16 * V * D * 4
+    # dh of one row over 2^24 columns: 256 slices
+    V, D = 1 << 24, 19456
+    assert f(1, V, D, 1, 1) >= D * 2 + V * 2 + 256 * D * 4
+
+
 class _Torch:
     """Streams without a GPU."""
     class cuda:
