@@ -545,8 +545,8 @@ int64_t sn_add_rmsnorm_backward_workspace_bytes(int32_t R, int32_t D);
  *   h : (N, D) and w : (V, D) of `dtype`: BF16 (tensor-core products of the
  *       values, summed in fp32), or F32 (each value split into three bf16
  *       parts, six products of the parts: fp32 accuracy; finite values beyond
- *       2^100 in magnitude count as 2^100, and infinite ones in rows that are
- *       not masked give NaN).  The tensor cores cut their fp32 sums, by up to
+ *       2^100 in magnitude count as 2^100, and an infinite one in a row that is
+ *       not masked gives NaN where a part that it meets is 0).  The tensor cores cut their fp32 sums, by up to
  *       2^-24 of the running sum every 16 terms, where an addition would round:
  *       no more than 2048 terms of a BF16 logit, 512 of an F32 one and 16384 of
  *       a BF16 gradient are summed like that before the sum is carried on by

@@ -22,7 +22,7 @@ namespace {
 constexpr int A_BYTES = 128 * BK * 2;      // 128 rows of w (or 128 columns x 64 rows)
 constexpr int EPI_WARPS = 8;               // two for each 32 rows of the tile, half of the columns each
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int MAX_SEG = 4;                 // segments of a sum in tensor memory
+constexpr int SEG = 8, MAX_SEG = 4;        // k blocks of a segment of a logit's sum, segments in tensor memory
 
 template <int NB>
 struct Few {
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int cta = blockIdx.x, ctas = gridDim.x;
     int first;
     const int items = item_count<EPI>(g, cta, ctas, &first);
-    // logits: segments of at least 8 blocks, at most MAX_SEG (see SEG in linear_ce.cu)
-    const int seg = EPI == EPI_OUT ? 1 << 30 : max(8, (g.kblocks + MAX_SEG - 1) / MAX_SEG);
+    // logits: segments (see SEG in linear_ce.cu), read out and added whenever there are MAX_SEG of them
+    constexpr int seg = EPI == EPI_OUT ? 1 << 30 : SEG, pass = EPI == EPI_OUT ? 1 << 30 : SEG * MAX_SEG;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < F::STAGES; ++i) {
@@ -180,37 +180,40 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 1) {
         if (lane == 0) {
             constexpr uint32_t idesc = pair::idesc_bf16(128, NB, AMN, false);
-            int s = 0;
+            int s = 0, turn = 0;   // passes so far
             uint32_t ph = 0;
             bool ok = true;
             for (int i = 0; i < items && ok; ++i) {
                 const Item t = item_of<EPI>(g, i, first, cta, ctas);
-                const int buf = i & 1;
-                if (!mbar_wait(&acc_empty[buf], ((i >> 1) & 1) ^ 1, limit)) {
-                    give_up(6);
-                    break;
-                }
-                tc::fence_after_sync();
-                for (int k = t.k0; k < t.k1; ++k) {
-                    if (!mbar_wait(&full[s], ph, limit)) {
-                        give_up(7);
+                for (int p0 = t.k0; p0 < t.k1 && ok; p0 += pass, ++turn) {
+                    const int buf = turn & 1, p1 = min(t.k1, p0 + pass);
+                    if (!mbar_wait(&acc_empty[buf], ((turn >> 1) & 1) ^ 1, limit)) {
+                        give_up(6);
                         ok = false;
                         break;
                     }
-                    const uint32_t a = stage0 + s * F::STAGE, b = a + A_BYTES;
-                    const int kk = k - t.k0, sg = kk / seg;
-                    const uint32_t d = tmem + buf * 256 + sg * NB;
+                    tc::fence_after_sync();
+                    for (int k = p0; k < p1; ++k) {
+                        if (!mbar_wait(&full[s], ph, limit)) {
+                            give_up(7);
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t a = stage0 + s * F::STAGE, b = a + A_BYTES;
+                        const int kk = k - p0, sg = kk / seg;
+                        const uint32_t d = tmem + buf * 256 + sg * NB;
 #pragma unroll
-                    for (int j = 0; j < BK / 16; ++j)
-                        mma_one(d, AMN ? pair::desc_mn_major(a + j * 2048) : pair::desc_k_major(a + j * 32),
-                                pair::desc_k_major(b + j * 32), idesc, kk - sg * seg > 0 || j > 0);
-                    tc::commit(&empty[s]);
-                    if (++s == F::STAGES) {
-                        s = 0;
-                        ph ^= 1;
+                        for (int j = 0; j < BK / 16; ++j)
+                            mma_one(d, AMN ? pair::desc_mn_major(a + j * 2048) : pair::desc_k_major(a + j * 32),
+                                    pair::desc_k_major(b + j * 32), idesc, kk - sg * seg > 0 || j > 0);
+                        tc::commit(&empty[s]);
+                        if (++s == F::STAGES) {
+                            s = 0;
+                            ph ^= 1;
+                        }
                     }
+                    if (ok) tc::commit(&acc_full[buf]);
                 }
-                if (ok) tc::commit(&acc_full[buf]);
             }
         }
     } else {
@@ -224,26 +227,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             mx[c] = -INFINITY;
             sum[c] = 0.0f;
         }
+        int turn = 0;
+        bool ok = true;
         for (int i = 0; i < items; ++i) {
             const Item t = item_of<EPI>(g, i, first, cta, ctas);
-            const int buf = i & 1, segs = (t.k1 - t.k0 - 1) / seg + 1;
-            if (!__all_sync(FULL, mbar_wait(&acc_full[buf], (i >> 1) & 1, limit))) {
-                if (lane == 0) give_up(8);
-                break;
-            }
-            tc::fence_after_sync();
             float v[CW];
-            const uint32_t acc = tmem + buf * 256 + c0 + ((uint32_t)quad << 21);
-            ld_cols(acc, v);
-            for (int q = 1; q < segs; ++q) {
-                float u[CW];
-                ld_cols(acc + q * NB, u);
+            for (int p0 = t.k0; p0 < t.k1; p0 += pass, ++turn) {
+                const int buf = turn & 1, segs = (min(t.k1 - p0, pass) - 1) / seg + 1;
+                if (!__all_sync(FULL, mbar_wait(&acc_full[buf], (turn >> 1) & 1, limit))) {
+                    if (lane == 0) give_up(8);
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+                const uint32_t acc = tmem + buf * 256 + c0 + ((uint32_t)quad << 21);
+                const int q0 = p0 == t.k0 ? 1 : 0;
+                if (q0 == 1) ld_cols(acc, v);
+                for (int q = q0; q < segs; ++q) {
+                    float u[CW];
+                    ld_cols(acc + q * NB, u);
 #pragma unroll
-                for (int c = 0; c < CW; ++c) v[c] += u[c];
+                    for (int c = 0; c < CW; ++c) v[c] += u[c];
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[buf]);
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[buf]);
+            if (!ok) break;
             const int r = t.r0 + quad * 32 + lane;
             const bool in = r < t.r1;
 #pragma unroll
