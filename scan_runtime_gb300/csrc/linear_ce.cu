@@ -16,6 +16,7 @@
 // x1y0, x1y1, x0y2 and x2y0, 2^-8 of it and less, together; the dropped ones are
 // below 2^-24).
 #include <algorithm>
+#include <climits>
 #include <cstring>
 
 #include "linear_ce.cuh"
@@ -52,7 +53,7 @@ struct CeGemm {
     float scale;
     float2* part;        // LSE: (ceil(N / min(bw, 128)), M) maximum (log2 space) and sum of so many columns
     float* zt;           // LSE: (M,) target logit
-    const float *lse, *g;
+    const float *lse, *g, *gmant;   // DZ, OUT: gmant is the factor that dz leaves out
     int planes;          // bf16 parts of the operands, and of dz
     // OUT (and DZ, whose output the tensor map `to` describes): through shared
     // memory and TMA where `tma`, else element by element
@@ -531,7 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        const float gmant = mantissa(g.scale, g.g);
+        const float gmant = EPI == EPI_LSE ? 1.0f : *g.gmant;
         const uint32_t box = stage0 + 12 * BLOCK + (warp - 2) * OUT_BOX;
         uint32_t used[2] = {0, 0};
         int turn = 0;
@@ -624,15 +625,51 @@ struct Packed {
     bf16* out;             // (planes, rows, ld)
     const void* targets;
 };
+// The factor that dz leaves out, in a gradient (see mantissa).
+struct Factor {
+    float scale;
+    const float* g;
+    float* out;            // NULL: a forward pass
+};
+// By one CTA: rows 1024 at a time until one has a gradient.
+__device__ void find_factor(const Factor& f, const Packed& h, int ids_type, int V) {
+    __shared__ int first;
+    if (threadIdx.x == 0) first = INT_MAX;
+    __syncthreads();
+    float m = f.g == nullptr ? mantissa(f.scale) : 0.0f;
+    for (int64_t r0 = 0; f.g != nullptr && r0 < h.rows; r0 += 1024) {
+        int mine = INT_MAX;
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const int64_t r = r0 + 256 * i + threadIdx.x;
+            if (r >= h.rows) continue;
+            const int64_t id = load_id(h.targets, ids_type, r);
+            if (mantissa(f.scale * f.g[r]) != 0.0f && id >= 0 && id < V) mine = (int)r;
+        }
+        if (mine != INT_MAX) atomicMin(&first, mine);
+        if (__syncthreads_or(mine != INT_MAX)) {
+            m = mantissa(f.scale * f.g[first]);
+            break;
+        }
+    }
+    if (threadIdx.x == 0) *f.out = m == 0.0f ? 1.0f : m;
+}
+
 // h and w in one launch: the first `first` CTAs have h, the others w (two
-// launches cost 2 us more).
+// launches cost 2 us more); in a gradient one more has the factor of dz.
 template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(Packed h, Packed w, int first, int D, int ld, int planes, int ids_type,
-                                                   int V) {
+__global__ void __launch_bounds__(256) pack_kernel(Packed h, Packed w, Factor f, int first, int D, int ld, int planes,
+                                                   int ids_type, int V) {
+    if (f.out != nullptr && blockIdx.x == gridDim.x - 1) {
+        pdl_trigger();
+        pdl_wait();
+        find_factor(f, h, ids_type, V);
+        return;
+    }
     const bool is_h = (int)blockIdx.x < first;
     const Packed a = is_h ? h : w;
     const T* x = static_cast<const T*>(a.x);
-    const int per = ld / 8, cta = is_h ? blockIdx.x : blockIdx.x - first, ctas = is_h ? first : gridDim.x - first;
+    const int per = ld / 8, cta = is_h ? blockIdx.x : blockIdx.x - first, ctas = is_h ? first : gridDim.x - (f.out != nullptr) - first;
     const int64_t items = a.rows * per, step = (int64_t)ctas * 256, plane = a.rows * ld;
     pdl_trigger();
     pdl_wait();
@@ -809,7 +846,7 @@ struct Plan {
     int bw_z;                   // tiles of the logits: forward, or one piece of dz
     Cut h, w;                   // dh over one piece, dw of one piece
     bool dh_slices;
-    int64_t o_h, o_w, o_part, o_zt, o_dz, o_dh, o_dw, total;
+    int64_t o_gmant, o_h, o_w, o_part, o_zt, o_dz, o_dh, o_dw, total;
 };
 
 // Partial maxima and sums of a row's logits.
@@ -828,6 +865,7 @@ Plan plan_for(int N, int V, int D, int dtype, bool backward) {
         at += r256(bytes);
         return o;
     };
+    p.o_gmant = backward ? take(4) : 0;
     p.o_h = p.pack_h ? take((int64_t)p.planes * N * p.ld * 2) : 0;
     p.o_w = p.pack_w ? take((int64_t)p.planes * V * p.ld * 2) : 0;
     const int kd = (D + BK - 1) / BK;
@@ -912,14 +950,14 @@ cudaError_t run_gemm(const CUtensorMap& ta, const CUtensorMap& tb, const CUtenso
                         : launch_gemm<EPI, AMN, BMN, NARROW>(ta, tb, to, g, st, limit, s);
 }
 
-cudaError_t pack(const Packed& h, const Packed& w, int D, int ld, int dtype, int planes, int ids_type, int V,
+cudaError_t pack(const Packed& h, const Packed& w, const Factor& f, int D, int ld, int dtype, int planes, int ids_type, int V,
                  cudaStream_t s) {
     auto ctas = [&](const Packed& a) { return (a.rows * (ld / 8) + 255) / 256; };
     const int64_t nh = ctas(h), nw = ctas(w), most = SMS * 8;
     const int64_t first = nh + nw <= most || nw == 0 ? std::min(nh, most)
                                                      : std::max<int64_t>(1, std::min(most - 1, most * nh / (nh + nw)));
-    const unsigned grid = (unsigned)std::min(nh + nw, most);
-    return launch_after(dtype == SN_DTYPE_F32 ? pack_kernel<float> : pack_kernel<bf16>, grid, 256, 0, 1, s, h, w, (int)first,
+    const unsigned grid = (unsigned)std::min(nh + nw, most) + (f.out != nullptr);
+    return launch_after(dtype == SN_DTYPE_F32 ? pack_kernel<float> : pack_kernel<bf16>, grid, 256, 0, 1, s, h, w, f, (int)first,
                         D, ld, planes, ids_type, V);
 }
 
@@ -976,7 +1014,8 @@ cudaError_t launch_linear_ce(const LinearCeArgs& x, void* ws, SnDevStatus* st, u
     if (p.pack_h) {
         Packed ph{x.N, x.h, (bf16*)(w0 + p.o_h), x.backward ? x.targets : nullptr}, pw{};
         if (p.pack_w) pw = Packed{x.V, x.w, (bf16*)(w0 + p.o_w), nullptr};
-        e = pack(ph, pw, x.D, p.ld, x.dtype, p.planes, x.ids_type, x.V, s);
+        const Factor f{x.logit_scale, x.grad_loss, x.backward ? (float*)(w0 + p.o_gmant) : nullptr};
+        e = pack(ph, pw, f, x.D, p.ld, x.dtype, p.planes, x.ids_type, x.V, s);
         if (e != cudaSuccess) return e;
         h = ph.out;
         if (p.pack_w) w = pw.out;
@@ -993,6 +1032,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs& x, void* ws, SnDevStatus* st, u
     g.scale = x.logit_scale;
     g.splits = 1;
     g.g = x.grad_loss;
+    g.gmant = (const float*)(w0 + p.o_gmant);
     CeGemm z = g;       // the logits
     z.M = x.N;
     z.kblocks = kd;
@@ -1009,6 +1049,7 @@ cudaError_t launch_linear_ce(const LinearCeArgs& x, void* ws, SnDevStatus* st, u
         few.scale = x.logit_scale;
         few.lse = x.lse;
         few.g = x.grad_loss;
+        few.gmant = g.gmant;
         if (!map_bf16(&mhf, h, p.ld, x.N, 1, p.ld, hplane, few_box(x.N))) return cudaErrorInvalidValue;
     }
     if (!x.backward) {

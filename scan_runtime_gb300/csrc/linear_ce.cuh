@@ -28,14 +28,14 @@ __device__ __forceinline__ int64_t load_id(const void* ids, int type, int64_t i)
     return type == SN_INDEX_I32 ? (int64_t)static_cast<const int32_t*>(ids)[i] : static_cast<const int64_t*>(ids)[i];
 }
 
-// dz carries logit_scale * grad_loss without this factor in [1, 2), which the
-// products' epilogues put back: where all rows have the same gradient (a mean
-// over the batch) and p_t is small, dz_t is then near a power of two and
-// loses next to nothing in bf16, instead of the same rounding in every row.
-__device__ __forceinline__ float mantissa(float scale, const float* g) {
-    const uint32_t b = __float_as_uint(scale * (g != nullptr ? g[0] : 1.0f));
-    const uint32_t e = (b >> 23) & 0xff;
-    return e == 0 || e == 0xff ? 1.0f : __uint_as_float((b & 0x7fffff) | 0x3f800000);
+// dz carries logit_scale * grad_loss without a factor in [1, 2), which the
+// products' epilogues put back: that of the first row with a gradient.  Where
+// all rows have the same one (a mean over the batch, over its unmasked part)
+// and p_t is small, dz_t is then near a power of two and loses next to nothing
+// in bf16, instead of the same rounding in every row.  0: x has no such factor.
+__device__ __forceinline__ float mantissa(float x) {
+    const uint32_t b = __float_as_uint(x), e = (b >> 23) & 0xff;
+    return e == 0 || e == 0xff ? 0.0f : __uint_as_float((b & 0x7fffff) | 0x3f800000);
 }
 
 // A running maximum (in log2 space) and sum of exponentials, joined with another.
@@ -72,7 +72,7 @@ struct CeFew {
     float scale;
     float2* part;            // LSE: (FEW_PARTS, N)
     float* zt;               // LSE: (N,)
-    const float *lse, *g;
+    const float *lse, *g, *gmant;   // DZ, OUT: gmant is the factor that dz leaves out
     bf16* dz;                // DZ: (N, ldz)
     int64_t ldz;
     float* out;              // OUT: (splits, N, ldo) fp32

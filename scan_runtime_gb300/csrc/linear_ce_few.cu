@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 1) tc::tmem_alloc(&tslot, 512);
     pdl_trigger();
     pdl_wait();
-    const float gmant = EPI == EPI_LSE ? 1.0f : mantissa(g.scale, g.g);
+    const float gmant = EPI == EPI_LSE ? 1.0f : *g.gmant;
     if (EPI != EPI_OUT && threadIdx.x < NB) {
         int target = -1;
         float lse2 = 0.0f, gs = 0.0f;
