@@ -41,12 +41,13 @@ __global__ void __launch_bounds__(256) embed_kernel(int n, int V, int D, const I
     pdl_trigger();
     pdl_wait();
     for (int64_t i0 = blockIdx.x * blockDim.y + threadIdx.y; i0 < n; i0 += (int64_t)step * AT_ONCE) {
-        float v[AT_ONCE][PER] = {};
+        float v[AT_ONCE][PER] = {}, times[AT_ONCE] = {};   // padding's zeros meet no scale (0 x inf = NaN)
 #pragma unroll
         for (int k = 0; k < AT_ONCE; ++k) {
             const int64_t i = i0 + (int64_t)k * step;
             const int row = i < n ? token_row(ids, i, V) : -1;
             if (row < 0) continue;
+            times[k] = scale;
             const T* p = table + (int64_t)row * D;
             if constexpr (VEC) {
                 if (c < D) load8(p + c, v[k]);
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(256) embed_kernel(int n, int V, int D, const I
             if (i >= n) break;
             Y* o = out + i * D;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) v[k][e] *= scale;
+            for (int e = 0; e < PER; ++e) v[k][e] *= times[k];
             if constexpr (VEC) {
                 if (c < D) store8(o + c, v[k]);
             } else {

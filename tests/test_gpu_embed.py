@@ -286,3 +286,17 @@ def test_memory_used_on_another_stream_is_not_handed_out(ctx, as_handle):
     assert s.query() or all(x.data_ptr() != at for x in others)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("odt", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 33])
+@pytest.mark.parametrize("scale", [float("inf"), float("-inf"), float("nan"), -2.0])
+def test_padding_is_zeros_whatever_the_scale(ctx, odt, D, scale):
+    g = _gen(67)
+    table = _normal(g, 20, D)
+    ids = torch.tensor([3, -1, 20, 7, 2 ** 40, 19], device="cuda")
+    out = ctx.embed(ids, table, scale=scale, dtype=odt)
+    pad = torch.tensor([1, 2, 4], device="cuda")
+    assert bool((out[pad] == 0).all())
+    rows = (table[ids[[0, 3, 5]]] * scale).to(odt)
+    assert torch.equal(out[[0, 3, 5]].nan_to_num(nan=5.0), rows.nan_to_num(nan=5.0))
