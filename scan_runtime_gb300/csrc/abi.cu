@@ -200,6 +200,7 @@ namespace {
 std::mutex g_attr_mutex;
 std::set<std::pair<const void*, int>> g_smem_set;                       // (kernel, device)
 std::map<std::tuple<const void*, int, int, size_t>, int> g_occupancy;   // (kernel, device, threads, smem)
+std::map<std::tuple<const void*, int, int, size_t, int>, bool> g_clusters;   // the same and the cluster's size
 }  // namespace
 
 cudaError_t set_smem_attr_once(const void* kern, size_t bytes) {
@@ -228,6 +229,40 @@ cudaError_t occupancy_once(const void* kern, int threads, size_t smem, int* out)
         if (occ < 1) return cudaErrorInvalidConfiguration;
     }
     *out = occ;
+    return cudaSuccess;
+}
+
+cudaError_t large_cluster_once(const void* kern, int threads, size_t smem, int cluster, bool* fits) {
+    cudaError_t e = set_smem_attr_once(kern, smem);
+    if (e != cudaSuccess) return e;
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_attr_mutex);
+    const auto key = std::make_tuple(kern, dev, threads, smem, cluster);
+    auto it = g_clusters.find(key);
+    if (it == g_clusters.end()) {
+        // more than eight CTAs have to be asked for
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = cluster;
+        cfg.blockDim = threads;
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at{};
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = (unsigned)cluster;
+        at.val.clusterDim.y = at.val.clusterDim.z = 1;
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        int count = 0;
+        if (cudaOccupancyMaxActiveClusters(&count, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();   // a size that the device does not know
+            count = 0;
+        }
+        it = g_clusters.emplace(key, count > 0).first;
+    }
+    *fits = it->second;
     return cudaSuccess;
 }
 }  // namespace sn

@@ -532,7 +532,8 @@ int64_t r256(int64_t x) { return (x + 255) / 256 * 256; }
 
 // CTAs of the sort: what more CTAs save in counting and placing they cost in
 // barriers (65536 tokens, 65536 rows: 46 us with 8 and 37 with 16 for the whole
-// gradient of 8 columns; 8192: 23 and 25).  A cluster has at most 16.
+// gradient of 8 columns; 8192: 23 and 25).  A cluster has at most 16, or 8 where
+// the device has no room for more.
 int sort_ctas(int n) { return n <= 2048 ? 1 : n < 32768 ? 8 : MAX_SORT_CTAS; }
 
 // Items of a unit: 64 where that still gives every SM 16 units (262144 tokens,
@@ -590,10 +591,13 @@ cudaError_t launch_embed_backward(const EmbedBwdArgs& x, void* ws, cudaStream_t 
     const void* k = x.ids_type == SN_INDEX_I32 ? (const void*)sort_kernel<int32_t> : (const void*)sort_kernel<int64_t>;
     cudaError_t e = set_smem_attr_once(k, SORT_SMEM);
     if (e != cudaSuccess) return e;
-    const int ctas = sort_ctas(x.n);
-    // more than 8 CTAs in a cluster have to be asked for
-    if (ctas > 8) e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+    int ctas = sort_ctas(x.n);
+    if (ctas > 8) {
+        bool fits = false;
+        e = large_cluster_once(k, SORT_T, SORT_SMEM, ctas, &fits);
+        if (e != cudaSuccess) return e;
+        if (!fits) ctas = 8;
+    }
     e = launch_after(x.ids_type == SN_INDEX_I32 ? sort_kernel<int32_t> : sort_kernel<int64_t>, ctas, SORT_T, SORT_SMEM, ctas,
                      s, q);
     if (e != cudaSuccess) return e;

@@ -75,6 +75,9 @@ cudaError_t set_smem_attr_once(const void* kern, size_t bytes);
 // Resident CTAs per SM of `kern` in CTAs of `threads` threads and `smem` bytes of
 // dynamic shared memory on the current device (cached for each of them).
 cudaError_t occupancy_once(const void* kern, int threads, size_t smem, int* out);
+// Whether the current device has room for clusters of `cluster` such CTAs, more
+// than the portable eight (cached likewise; a partition of a GPU may not).
+cudaError_t large_cluster_once(const void* kern, int threads, size_t smem, int cluster, bool* fits);
 
 
 // tensor-map encoder (driver entry point fetched through the runtime)

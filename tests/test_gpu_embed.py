@@ -300,3 +300,14 @@ def test_padding_is_zeros_whatever_the_scale(ctx, odt, D, scale):
     assert bool((out[pad] == 0).all())
     rows = (table[ids[[0, 3, 5]]] * scale).to(odt)
     assert torch.equal(out[[0, 3, 5]].nan_to_num(nan=5.0), rows.nan_to_num(nan=5.0))
+
+
+def test_many_tokens_take_a_cluster_of_sixteen(ctx):
+    """Where the device grants it, as a whole GB300 does."""
+    from tests._graph_nodes import nodes
+    for n, ctas in ((2048, 1), (32767, 8), (32768, 16)):
+        ids = torch.zeros(n, dtype=torch.int64, device="cuda")
+        rows = torch.ones(n, 8, device="cuda")
+        ctx.embed_backward(ids, rows, 4)
+        kernels, _ = nodes(lambda: ctx.embed_backward(ids, rows, 4))
+        assert [k.grid[0] for k in kernels if "sort_kernel" in k.name] == [ctas]
