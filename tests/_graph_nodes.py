@@ -16,16 +16,17 @@ class _KernelParams(ctypes.Structure):      # CUDA_KERNEL_NODE_PARAMS_v2
 
 class Kernel:
     def __init__(self, name, grid, block):
-        self.name, self.grid, self.block = name, grid, block
+        self.name, self.grid, self.block, self.ints = name, grid, block, ()
 
 
 def _ok(result):
     assert result == 0, f"CUDA driver error {result}"
 
 
-def nodes(call):
+def nodes(call, ints=None):
     """Kernels of the graph that ``call()`` is captured in (on the current stream, which it has to use), and the
-    number of its memsets.  The graph is not run."""
+    number of its memsets.  The graph is not run.  ``ints``: (part of a kernel's name, index of a parameter, count)
+    reads the first so many 32-bit integers of that parameter of such kernels."""
     cu = ctypes.CDLL("libcuda.so.1")
     p, ref = ctypes.c_void_p, ctypes.byref
     s = torch.cuda.Stream()
@@ -57,5 +58,8 @@ def nodes(call):
             else:
                 _ok(cu.cuKernelGetName(ref(name), p(k.kern)))
             kernels.append(Kernel(name.value.decode(), tuple(k.grid), tuple(k.block)))
+            if ints is not None and ints[0] in kernels[-1].name:
+                params = ctypes.cast(k.params, ctypes.POINTER(p))
+                kernels[-1].ints = tuple(ctypes.cast(params[ints[1]], ctypes.POINTER(ctypes.c_int))[:ints[2]])
     _ok(cu.cuGraphDestroy(graph))
     return kernels, memsets

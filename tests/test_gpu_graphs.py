@@ -212,3 +212,48 @@ def test_scan_replayed_across_a_growth(sr, ctx, which):
         assert torch.equal(out, want)
         assert torch.equal(ctx.scan_fma(a, b)[0], want)
         head()
+
+
+def _captured(call):
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    return graph, out
+
+
+@pytest.mark.parametrize("n,V,D,dt", [(1, 300, 768, BF16), (1024, 300, 33, torch.float32), (40000, 64, 16, BF16)])
+def test_lookup_and_its_gradient_replayed(ctx, n, V, D, dt):
+    """On new ids and rows each time, one and eight and sixteen CTAs sorting."""
+    g = torch.Generator("cuda").manual_seed(n)
+    table, rows = torch.randn(V, D, generator=g, device="cuda").to(dt), torch.empty(n, D, dtype=dt, device="cuda")
+    ids = torch.zeros(n, dtype=torch.int64, device="cuda")
+    graph, got = _captured(lambda: (ctx.embed(ids, table, scale=3.0), ctx.embed_backward(ids, rows, V, scale=3.0)))
+    for _ in range(3):
+        ids.copy_(torch.randint(-2, V, (n,), generator=g, device="cuda"))
+        rows.normal_(generator=g)
+        graph.replay()
+        want = ctx.embed(ids, table, scale=3.0), ctx.embed_backward(ids, rows, V, scale=3.0)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("R,D,dt", [(1, 2048, BF16), (300, 511, BF16), (2000, 1536, torch.float32)])
+def test_norm_and_its_gradient_replayed(ctx, R, D, dt):
+    g = torch.Generator("cuda").manual_seed(R)
+    x, r, c = (torch.empty(R, D, dtype=dt, device="cuda") for _ in range(3))
+    w = torch.rand(D, generator=g, device="cuda")
+
+    def step():
+        q, scales, _, _ = ctx.add_rmsnorm(x, r, w, eps=1e-6, dtype=torch.float8_e4m3fn, group=128)
+        y, _, h, rstd = ctx.add_rmsnorm(x, r, w, eps=1e-6, rstd=True)
+        return (q.view(torch.uint8), scales, y, h, rstd, *ctx.add_rmsnorm_backward(y, h, w, rstd, c))
+
+    for t in (x, r, c):
+        t.normal_(generator=g)
+    graph, got = _captured(step)
+    for _ in range(3):
+        for t in (x, r, c):
+            t.normal_(generator=g)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
