@@ -26,7 +26,6 @@ enum SnKernelId : int {
     SN_K_RECUR_DECODE = 4,
     SN_K_RECUR_CHUNK = 5,
     SN_K_LINEAR_CE = 6,
-    SN_K_EMBED_SORT = 7,
 };
 
 struct SnCtx {
