@@ -311,3 +311,21 @@ def test_many_tokens_take_a_cluster_of_sixteen(ctx):
         ctx.embed_backward(ids, rows, 4)
         kernels, _ = nodes(lambda: ctx.embed_backward(ids, rows, 4))
         assert [k.grid[0] for k in kernels if "sort_kernel" in k.name] == [ctas]
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_by_its_handles(ctx, handle):
+    """0 and 1 (cudaStreamLegacy) while another stream is the current one."""
+    g = _gen(71)
+    ids = torch.randint(-1, 50, (300,), generator=g, device="cuda")
+    rows = _normal(g, 300, 40)
+    want = ctx.embed_backward(ids, rows, 50)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        used = rows.clone()
+        s.synchronize()
+        got = ctx.embed_backward(ids, used, 50, stream=handle)
+        del used
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
