@@ -793,7 +793,8 @@ int64_t r256(int64_t x) { return (x + 255) / 256 * 256; }
 // off by 7e-7 of itself, measured).  bf16 gradients, and the five small products
 // of fp32 ones, are summed whole, but at most MOST_BLOCKS at a time, longer sums
 // in splits that are added in fp32: 1024 steps cut 2^-14 at most, a thirtieth of
-// bf16's half step.
+// bf16's half step (the gradient of 8000 x 32768 x 1024 takes 980 us with two
+// splits of dh, 950 with one).
 constexpr int SEG = 8, WHOLE = 32;
 
 // dz of one piece of the vocabulary takes at most this much workspace.
